@@ -15,7 +15,8 @@
 // so every instruction has 128 full rows whatever R is, each thread of a warpgroup owns one token of a tile, its page's
 // exponents are two factors of that thread (K's on its scores, V's on its weights), and the row sums stay in registers.
 // The softmax's reference value is per row and for all tokens of an accumulator: it is the running maximum of score +
-// V's exponent, raised (with the accumulator rescaled) only when a tile exceeds it by more than a factor 2^kSlack.
+// V's exponent, raised (with the accumulator rescaled) only when a tile exceeds it by more than a factor 2^kSlack.  A row's
+// first visible token sets it, however far below zero its score lies and whichever tile of the part it is in.
 //
 // A warp that walks a block's share publishes each item's part as a job before it loads its tiles, so the softmax warps
 // stage the next job's queries while the last product of the one before is under way.
@@ -56,7 +57,6 @@ constexpr int kItemCost = 4;               // what an item costs beside its tile
 constexpr int kSlack = 5;                  // log2 by which weights may exceed 1 before their reference value is raised
 constexpr float kPUnit = 8.f;              // weight 1 as an e4m3 operand: 8 * 2^kSlack = 256 <= 448
 constexpr float kRest = 4096.f;            // scale of the weights' low parts: 8 * 4096 <= 57344, e5m2's largest
-constexpr float kUnset = -1e4f;            // reference value of a row that no token of a tile was visible to
 constexpr long long kWaitNs = 2000000000;  // bound on any wait
 constexpr int kMergeRows = 8;              // warps of a block of the joining launch
 
@@ -305,7 +305,8 @@ template <int R, int kSlots>
 struct __align__(16) Shared {
   float qf[2][R], ref[2][R];               // of this job and the next: factor on a row's scores, minus its reference value
   float peak[4][R];                        // per warp: largest score of a row, then its sum
-  float f[R];                              // rise of a row's reference value, then factor on its outputs
+  float f[R], fall[R];                     // rise of a row's reference value, then factor on its outputs; factor on what it has so far
+  int unset[R];                            // the row has seen no token yet
   int head[2][R];                          // a row's place in a sequence's block: row * Hq + head
   unsigned long long path[64], seen[kJobs][64];     // rows of the row block that see a token of the block, a bit each
   Job job[kJobs];
@@ -756,6 +757,7 @@ __global__ void __launch_bounds__(Layout<R, D>::kThreads, 2)
       float2 sum[RT / 2];                                  // of rows 2i and 2i + 1
 #pragma unroll
       for (int r = 0; r < RT / 2; ++r) sum[r] = make_float2(0.f, 0.f);
+      bool open = true;                                    // a row of the warpgroup is unset
 #pragma unroll 1
       for (int i = 0; i < count; ++i) {
         mbar_wait(&sh.full[v_slot], v_turn & 1, dead);
@@ -805,8 +807,9 @@ __global__ void __launch_bounds__(Layout<R, D>::kThreads, 2)
         float top = -INFINITY;
 #pragma unroll
         for (int r = 0; r < RT / 2; ++r) top = fmaxf(top, fmaxf(x[r].x, x[r].y));
-        if (group_or<L::kGroups>(grp, i == 0 || top + float(ev) > float(kSlack))) {
-          // a row's reference value rises to the tile's largest score + V's exponent
+        if (group_or<L::kGroups>(grp, open || top + float(ev) > float(kSlack))) {
+          // a row's reference value rises to the tile's largest score + V's exponent; an unset one becomes that, whatever
+          // its sign, and stays 0 while the tiles show the row nothing (-inf; a NaN row counts as set)
           float up = 0.f;
 #pragma unroll
           for (int r = 0; r < RT; ++r) {
@@ -815,15 +818,20 @@ __global__ void __launch_bounds__(Layout<R, D>::kThreads, 2)
           }
           if (lane < RT) sh.peak[quad][c0 + lane] = up;
           group_barrier<L::kGroups>(grp);
+          bool unset = false;
           if (t < RT) {
             const int r = c0 + t;
             up = fmaxf(fmaxf(sh.peak[0][r], sh.peak[1][r]), fmaxf(sh.peak[2][r], sh.peak[3][r]));
-            const float rise = fmaxf(up, i == 0 ? kUnset : 0.f);
+            unset = i == 0 || sh.unset[r];
+            const float rise = unset && up > -INFINITY ? up : fmaxf(up, 0.f);
+            unset = unset && up == -INFINITY;
+            sh.unset[r] = unset;
             sh.f[r] = rise;
+            sh.fall[r] = ex2(fminf(-rise, 0.f));           // (a row that was unset has nothing so far)
             ref[t] -= rise;
           }
           if (i > 0) mbar_wait(&sh.pv_done, (n - 1) & 1, dead);
-          group_barrier<L::kGroups>(grp);
+          open = group_or<L::kGroups>(grp, unset);
           tc_after();
 #pragma unroll
           for (int r = 0; r < RT; r += 8) {
@@ -842,8 +850,7 @@ __global__ void __launch_bounds__(Layout<R, D>::kThreads, 2)
               tc_wait_ld();
 #pragma unroll
               for (int e = 0; e < 4; ++e) {
-                const float2 rise = *reinterpret_cast<const float2*>(sh.f + c0 + r + 2 * e);
-                const float2 f = make_float2(ex2(-rise.x), ex2(-rise.y));
+                const float2 f = *reinterpret_cast<const float2*>(sh.fall + c0 + r + 2 * e);
                 sum[r / 2 + e] = mul2(sum[r / 2 + e], f);
                 hi[2 * e] *= f.x, hi[2 * e + 1] *= f.y;
                 lo[2 * e] *= f.x, lo[2 * e + 1] *= f.y;
