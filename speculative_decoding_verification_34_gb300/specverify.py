@@ -7,6 +7,7 @@ the shared library is missing this module raises instead of computing anything i
 """
 from __future__ import annotations
 
+import contextlib
 import ctypes
 import os
 from typing import Optional
@@ -150,6 +151,17 @@ def _stream(stream) -> Optional[int]:
     return stream.cuda_stream if hasattr(stream, "cuda_stream") else int(stream)
 
 
+def _on(stream):
+    """Context in which the call's stream is the current one.  A workspace allocated in it is filled before the call's kernels
+    run, and once dropped is not handed out again but to that stream, behind them."""
+    handle = _stream(stream)
+    if handle == torch.cuda.current_stream().cuda_stream:
+        return contextlib.nullcontext()
+    if not isinstance(stream, torch.cuda.Stream):        # (0 and 1: the legacy default stream)
+        stream = torch.cuda.default_stream() if handle in (None, 0, 1) else torch.cuda.ExternalStream(handle)
+    return torch.cuda.stream(stream)
+
+
 def spec_verify_workspace_bytes(B: int, gmax: int, V: int, dtype: int = SPEC_BF16) -> int:
     return int(load_library().spec_verify_workspace_bytes(B, gmax, V, dtype))
 
@@ -161,9 +173,10 @@ def alloc_workspace(B: int, gmax: int, V: int, dtype: int = SPEC_BF16, device=No
     return torch.zeros(max(n, 64), dtype=torch.uint8, device=device or "cuda")
 
 
-def _ws(workspace, B, gmax, V, code, device):
+def _ws(workspace, B, gmax, V, code, device, stream):
     if workspace is None:
-        workspace = alloc_workspace(B, gmax, V, code, device)
+        with _on(stream):
+            workspace = alloc_workspace(B, gmax, V, code, device)
     if workspace.dtype != torch.uint8:
         raise TypeError("workspace must be a uint8 tensor")
     return workspace, _ptr(workspace, "workspace"), workspace.numel()
@@ -177,7 +190,7 @@ def spec_verify_greedy(target_logits: torch.Tensor, draft_tokens: torch.Tensor,
     gmax = gp1 - 1
     lib = load_library()
     code = _dtype_code(target_logits)
-    ws, wsp, wsn = _ws(workspace, B, gmax, V, code, target_logits.device)
+    ws, wsp, wsn = _ws(workspace, B, gmax, V, code, target_logits.device, stream)
     _check(lib.spec_verify_greedy(
         _ptr(target_logits, "target_logits"), code,
         _ptr(draft_tokens, "draft_tokens", torch.int32, (B, gmax)),
@@ -199,7 +212,7 @@ def spec_verify_sample(target_logits: torch.Tensor, draft_logits: torch.Tensor,
         raise TypeError("target and draft logits must have the same dtype")
     lib = load_library()
     code = _dtype_code(target_logits)
-    ws, wsp, wsn = _ws(workspace, B, gmax, V, code, target_logits.device)
+    ws, wsp, wsn = _ws(workspace, B, gmax, V, code, target_logits.device, stream)
     _check(lib.spec_verify_sample(
         _ptr(target_logits, "target_logits"),
         _ptr(draft_logits, "draft_logits", None, (B, gmax, V)), code,
@@ -233,7 +246,7 @@ def spec_verify_greedy_commit(target_logits: torch.Tensor, draft_tokens: torch.T
     gmax = gp1 - 1
     lib = load_library()
     code = _dtype_code(target_logits)
-    ws, wsp, wsn = _ws(workspace, B, gmax, V, code, target_logits.device)
+    ws, wsp, wsn = _ws(workspace, B, gmax, V, code, target_logits.device, stream)
     _check(lib.spec_verify_greedy_commit(
         _ptr(target_logits, "target_logits"), code,
         _ptr(draft_tokens, "draft_tokens", torch.int32, (B, gmax)),
@@ -253,7 +266,7 @@ def _sample_commit_args(target_logits, draft_logits, draft_tokens, num_draft, te
     if draft_logits.dtype != target_logits.dtype:
         raise TypeError("target and draft logits must have the same dtype")
     code = _dtype_code(target_logits)
-    ws, wsp, wsn = _ws(workspace, B, gmax, V, code, target_logits.device)
+    ws, wsp, wsn = _ws(workspace, B, gmax, V, code, target_logits.device, stream)
     args = (_ptr(target_logits, "target_logits"),
             _ptr(draft_logits, "draft_logits", None, (B, gmax, V)), code,
             _ptr(draft_tokens, "draft_tokens", torch.int32, (B, gmax)),
@@ -300,7 +313,7 @@ def spec_verify_sample_truncated(target_logits: torch.Tensor, draft_logits: torc
         raise TypeError("target and draft logits must have the same dtype")
     lib = load_library()
     code = _dtype_code(target_logits)
-    ws, wsp, wsn = _ws(workspace, B, gmax, V, code, target_logits.device)
+    ws, wsp, wsn = _ws(workspace, B, gmax, V, code, target_logits.device, stream)
     _check(lib.spec_verify_sample_truncated(
         _ptr(target_logits, "target_logits"),
         _ptr(draft_logits, "draft_logits", None, (B, gmax, V)), code,
@@ -324,7 +337,7 @@ def _truncated_commit_args(target_logits, draft_logits, draft_tokens, num_draft,
     if draft_logits.dtype != target_logits.dtype:
         raise TypeError("target and draft logits must have the same dtype")
     code = _dtype_code(target_logits)
-    ws, wsp, wsn = _ws(workspace, B, gmax, V, code, target_logits.device)
+    ws, wsp, wsn = _ws(workspace, B, gmax, V, code, target_logits.device, stream)
     args = (_ptr(target_logits, "target_logits"),
             _ptr(draft_logits, "draft_logits", None, (B, gmax, V)), code,
             _ptr(draft_tokens, "draft_tokens", torch.int32, (B, gmax)),
@@ -376,7 +389,7 @@ def spec_verify_sample_truncated_split(saved_logits: torch.Tensor, block_logits:
         raise TypeError("target and draft logits must have the same dtype")
     lib = load_library()
     code = _dtype_code(saved_logits)
-    ws, wsp, wsn = _ws(workspace, B, gmax, V, code, saved_logits.device)
+    ws, wsp, wsn = _ws(workspace, B, gmax, V, code, saved_logits.device, stream)
     _check(lib.spec_verify_sample_truncated_split(
         _ptr(saved_logits, "saved_logits"), _ptr(block_logits, "block_logits"),
         _ptr(draft_logits, "draft_logits", None, (B, gmax, V)), code,
@@ -403,7 +416,7 @@ def spec_verify_tree_greedy(target_logits: torch.Tensor, node_tokens: torch.Tens
     nmax = np1 - 1
     lib = load_library()
     code = _dtype_code(target_logits)
-    ws, wsp, wsn = _ws(workspace, B, nmax, V, code, target_logits.device)
+    ws, wsp, wsn = _ws(workspace, B, nmax, V, code, target_logits.device, stream)
     _check(lib.spec_verify_tree_greedy(
         _ptr(target_logits, "target_logits"), code,
         _ptr(node_tokens, "node_tokens", torch.int32, (B, nmax)),
@@ -416,10 +429,10 @@ def spec_verify_tree_greedy(target_logits: torch.Tensor, node_tokens: torch.Tens
 
 
 def _tree_args(target_logits, node_tokens, node_parents, num_nodes, out_tokens, num_accepted, path_nodes, status,
-               workspace):
+               workspace, stream):
     B, np1, V = target_logits.shape
     nmax = np1 - 1
-    ws, wsp, wsn = _ws(workspace, B, nmax, V, _dtype_code(target_logits), target_logits.device)
+    ws, wsp, wsn = _ws(workspace, B, nmax, V, _dtype_code(target_logits), target_logits.device, stream)
     args = (_ptr(target_logits, "target_logits"), _dtype_code(target_logits),
             _ptr(node_tokens, "node_tokens", torch.int32, (B, nmax)),
             _ptr(node_parents, "node_parents", torch.int32, (B, nmax)),
@@ -442,7 +455,7 @@ def spec_verify_tree_greedy_commit(target_logits: torch.Tensor, node_tokens: tor
     """spec_verify_tree_greedy and spec_commit_kv_lengths (gmax = nmax) of the same round, fused."""
     B = target_logits.shape[0]
     args, _ = _tree_args(target_logits, node_tokens, node_parents, num_nodes, out_tokens, num_accepted, path_nodes,
-                         status, workspace)
+                         status, workspace, stream)
     _check(load_library().spec_verify_tree_greedy_commit(
         *args, *_commit_args(B, target_kv_len, draft_kv_len, correction_processed, history, committed_len),
         _stream(stream)))
@@ -454,7 +467,7 @@ def prepare_verify_tree_greedy_commit(target_logits, node_tokens, node_parents, 
                                       stream=None) -> "_Prepared":
     B = target_logits.shape[0]
     args, ws = _tree_args(target_logits, node_tokens, node_parents, num_nodes, out_tokens, num_accepted, path_nodes,
-                          status, workspace)
+                          status, workspace, stream)
     args = args + _commit_args(B, target_kv_len, draft_kv_len, correction_processed, history, committed_len) + \
         (_stream(stream),)
     keep = (target_logits, node_tokens, node_parents, num_nodes, out_tokens, num_accepted, path_nodes, status, ws,
@@ -467,7 +480,7 @@ def prepare_verify_tree_greedy(target_logits, node_tokens, node_parents, num_nod
     B, np1, V = target_logits.shape
     nmax = np1 - 1
     lib = load_library()
-    ws, wsp, wsn = _ws(workspace, B, nmax, V, _dtype_code(target_logits), target_logits.device)
+    ws, wsp, wsn = _ws(workspace, B, nmax, V, _dtype_code(target_logits), target_logits.device, stream)
     args = (_ptr(target_logits, "target_logits"), _dtype_code(target_logits),
             _ptr(node_tokens, "node_tokens", torch.int32, (B, nmax)),
             _ptr(node_parents, "node_parents", torch.int32, (B, nmax)),
@@ -500,7 +513,7 @@ def spec_verify_greedy_split(saved_logits: torch.Tensor, block_logits: Optional[
     B, gmax, V = _split_shapes(saved_logits, block_logits)
     lib = load_library()
     code = _dtype_code(saved_logits)
-    ws, wsp, wsn = _ws(workspace, B, gmax, V, code, saved_logits.device)
+    ws, wsp, wsn = _ws(workspace, B, gmax, V, code, saved_logits.device, stream)
     _check(lib.spec_verify_greedy_split(
         _ptr(saved_logits, "saved_logits"), _ptr(block_logits, "block_logits"), code,
         _ptr(draft_tokens, "draft_tokens", torch.int32, (B, gmax)),
@@ -524,7 +537,7 @@ def spec_verify_sample_split(saved_logits: torch.Tensor, block_logits: Optional[
         raise TypeError("target and draft logits must have the same dtype")
     lib = load_library()
     code = _dtype_code(saved_logits)
-    ws, wsp, wsn = _ws(workspace, B, gmax, V, code, saved_logits.device)
+    ws, wsp, wsn = _ws(workspace, B, gmax, V, code, saved_logits.device, stream)
     _check(lib.spec_verify_sample_split(
         _ptr(saved_logits, "saved_logits"), _ptr(block_logits, "block_logits"),
         _ptr(draft_logits, "draft_logits", None, (B, gmax, V)), code,
@@ -640,7 +653,7 @@ def prepare_verify_sample(target_logits, draft_logits, draft_tokens, num_draft, 
     B, gp1, V = target_logits.shape
     gmax = gp1 - 1
     lib = load_library()
-    ws, wsp, wsn = _ws(workspace, B, gmax, V, _dtype_code(target_logits), target_logits.device)
+    ws, wsp, wsn = _ws(workspace, B, gmax, V, _dtype_code(target_logits), target_logits.device, stream)
     args = (_ptr(target_logits, "target_logits"),
             _ptr(draft_logits, "draft_logits", target_logits.dtype, (B, gmax, V)),
             _dtype_code(target_logits),
@@ -664,7 +677,7 @@ def prepare_verify_greedy_commit(target_logits, draft_tokens, num_draft, out_tok
     B, gp1, V = target_logits.shape
     gmax = gp1 - 1
     code = _dtype_code(target_logits)
-    ws, wsp, wsn = _ws(workspace, B, gmax, V, code, target_logits.device)
+    ws, wsp, wsn = _ws(workspace, B, gmax, V, code, target_logits.device, stream)
     args = (_ptr(target_logits, "target_logits"), code,
             _ptr(draft_tokens, "draft_tokens", torch.int32, (B, gmax)),
             _ptr(num_draft, "num_draft", torch.int32, (B,)), B, gmax, V,
@@ -696,7 +709,7 @@ def prepare_verify_sample_truncated(target_logits, draft_logits, draft_tokens, n
     B, gp1, V = target_logits.shape
     gmax = gp1 - 1
     lib = load_library()
-    ws, wsp, wsn = _ws(workspace, B, gmax, V, _dtype_code(target_logits), target_logits.device)
+    ws, wsp, wsn = _ws(workspace, B, gmax, V, _dtype_code(target_logits), target_logits.device, stream)
     args = (_ptr(target_logits, "target_logits"),
             _ptr(draft_logits, "draft_logits", target_logits.dtype, (B, gmax, V)),
             _dtype_code(target_logits),
@@ -734,7 +747,7 @@ def prepare_verify_greedy(target_logits, draft_tokens, num_draft, out_tokens, nu
     B, gp1, V = target_logits.shape
     gmax = gp1 - 1
     lib = load_library()
-    ws, wsp, wsn = _ws(workspace, B, gmax, V, _dtype_code(target_logits), target_logits.device)
+    ws, wsp, wsn = _ws(workspace, B, gmax, V, _dtype_code(target_logits), target_logits.device, stream)
     args = (_ptr(target_logits, "target_logits"), _dtype_code(target_logits),
             _ptr(draft_tokens, "draft_tokens", torch.int32, (B, gmax)),
             _ptr(num_draft, "num_draft", torch.int32, (B,)), B, gmax, V,
@@ -965,7 +978,8 @@ def _attention_args(q, cache, page_table, kv_len, out, num_draft, node_parents, 
     if D != cache.head_dim:
         raise ValueError(f"q has head_dim {D}, the cache {cache.head_dim}")
     if workspace is None:
-        workspace = alloc_attention_workspace(B, gmax, Hq, cache.kv_heads, D, q.device)
+        with _on(stream):
+            workspace = alloc_attention_workspace(B, gmax, Hq, cache.kv_heads, D, q.device)
     if workspace.dtype != torch.uint8:
         raise TypeError("workspace must be a uint8 tensor")
     qp, qs = _strided(q, "q", (B, rows, Hq, D))
