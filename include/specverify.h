@@ -506,7 +506,8 @@ int spec_kv_keep_path(const spec_kv_cache_t* cache, const int32_t* page_table, i
  *   out            [B][rows][Hq][head_dim] bf16, contiguous, 4-byte aligned (written)
  *   status         [B] or NULL: bits are OR-ed in.  SPEC_ST_BAD_PAGE: positions whose page is not there, or that
  *                  lie behind the table, are seen by no row (a row that sees nothing is 0; a negative
- *                  kv_len leaves the sequence's rows as they were).  SPEC_ST_TIMEOUT: as for the verify calls
+ *                  kv_len leaves the sequence's rows as they were).  SPEC_ST_TIMEOUT: a wait ran out in a block
+ *                  that worked on the sequence; its computed rows are not defined, the workspace may be used again
  *   workspace      spec_attention_workspace_bytes(B, gmax, Hq, kv_heads, head_dim) bytes, 16-byte aligned; what it
  *                  holds before and after a call does not matter, but calls that may overlap need one each
  * Limits: gmax <= SPEC_MAX_TREE_NODES, Hq a multiple of kv_heads, head_dim 64 or 128.  Contents of cache slots

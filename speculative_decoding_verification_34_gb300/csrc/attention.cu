@@ -57,7 +57,11 @@ constexpr int kItemCost = 4;               // what an item costs beside its tile
 constexpr int kSlack = 5;                  // log2 by which weights may exceed 1 before their reference value is raised
 constexpr float kPUnit = 8.f;              // weight 1 as an e4m3 operand: 8 * 2^kSlack = 256 <= 448
 constexpr float kRest = 4096.f;            // scale of the weights' low parts: 8 * 4096 <= 57344, e5m2's largest
-constexpr long long kWaitNs = 2000000000;  // bound on any wait
+#ifndef SPEC_ATTENTION_WAIT_NS             // (shorter in a build that tests what follows)
+#define SPEC_ATTENTION_WAIT_NS 2000000000
+#endif
+constexpr long long kWaitNs = SPEC_ATTENTION_WAIT_NS;    // bound on a wait for another role of the block
+constexpr long long kDrainNs = 2000000000; // bound on a wait for copies and products in flight, before their memory is given up
 constexpr int kMergeRows = 8;              // warps of a block of the joining launch
 
 // An item that several blocks share, as the joining launch finds it.
@@ -117,13 +121,17 @@ __device__ __forceinline__ long long now_ns() {
   asm volatile("mov.u64 %0, %globaltimer;" : "=l"(t));
   return t;
 }
-// A bounded wait.  When it runs out it sets *dead and returns false: every role goes on to the end of what it holds (all
-// its accesses stay in bounds whatever the data, and the warps agree on the barriers to come), no later wait of the
-// block waits, no new job is taken, and the call reports SPEC_ST_TIMEOUT.
+// A bounded wait.  When it runs out it sets *dead and returns false, and no later wait of the block waits.  The block then
+// comes to its end: the role that loads and the one that issues products stop at their next wait, the softmax goes on to the
+// end of the job that it has taken, with accesses that stay in bounds whatever the data, and takes no other.  (A warp's lanes,
+// and the softmax warps together, agree on that: their barriers need one another.)  What is in flight lands before its memory
+// is given up, and every sequence of the block's share reports SPEC_ST_TIMEOUT: its rows may be unwritten, or joined from
+// partials that are.  A try holds a thread for 4 us at most, so a tile costs little once no wait waits.
 __device__ __forceinline__ bool mbar_wait(uint64_t* m, unsigned parity, volatile int* dead) {
-  if (mbar_try(m, parity)) return true;
+  auto done = [&] { return kWaitNs < 4000 ? mbar_test(m, parity) : mbar_try(m, parity); };
+  if (done()) return true;
   const long long t0 = now_ns();
-  while (!mbar_try(m, parity)) {
+  while (!done()) {
     if (*dead) return false;
     if (now_ns() - t0 > kWaitNs) {
       *dead = 1;
@@ -132,7 +140,14 @@ __device__ __forceinline__ bool mbar_wait(uint64_t* m, unsigned parity, volatile
   }
   return true;
 }
-// A softmax warpgroup's own barrier (1 or 2), one that also says whether any of its threads has x, and one of all of them.
+// Waits for what is in flight, whether or not the block gave up.
+__device__ __forceinline__ void mbar_drain(uint64_t* m, unsigned parity) {
+  const long long t0 = now_ns();
+  while (!mbar_try(m, parity) && now_ns() - t0 < kDrainNs) {
+  }
+}
+// A softmax warpgroup's own barrier (1 or 2), one that also says whether any of its threads has x, and one of all of them
+// that says whether every thread has x.
 template <int kId>
 __device__ __forceinline__ void barrier_of() {
   asm volatile("barrier.cta.sync %0, 128;" ::"n"(kId) : "memory");
@@ -158,8 +173,13 @@ __device__ __forceinline__ bool group_or(int grp, bool x) {
   return kGroups == 1 || grp == 0 ? or_of<1>(x) : or_of<2>(x);
 }
 template <int kCount>
-__device__ __forceinline__ void softmax_barrier() {
-  asm volatile("barrier.cta.sync 3, %0;" ::"n"(kCount) : "memory");
+__device__ __forceinline__ bool softmax_all(bool x) {
+  unsigned r;
+  asm volatile("{\n .reg .pred p, q;\n setp.ne.u32 q, %2, 0;\n barrier.cta.red.and.pred p, 3, %1, q;\n selp.u32 %0, 1, 0, p;\n}"
+               : "=r"(r)
+               : "n"(kCount), "r"(unsigned(x))
+               : "memory");
+  return r;
 }
 __device__ __forceinline__ void tma_page(const CUtensorMap* map, unsigned dst, uint64_t* bar, int y) {
   asm volatile(
@@ -313,12 +333,12 @@ struct __align__(16) Shared {
   int up[64];
   int slot[kSlots][8];                     // pages of a V slot's tile: exponents of K and V, or kNoPage
   uint64_t full[kSlots], empty[kSlots], job_full[kJobs], seen_full[kJobs], job_empty[kJobs];
-  uint64_t s_full, s_free, p_ready, pv_done, q_ready;
+  uint64_t s_full, s_free, p_ready, pv_done, q_ready, drained;
   unsigned tmem;
-  int dead, more[2];                       // a wait ran out; there is this job (by its parity)
+  int dead;                                // a wait ran out
   long long scan[10];
-  int start_b;
-  long long start_at;
+  int start_b;                             // the share: its first sequence, the first unit of that, units
+  long long start_at, share;
 };
 constexpr int kNoPage = INT_MIN;
 
@@ -509,6 +529,7 @@ __global__ void __launch_bounds__(Layout<R, D>::kThreads, 2)
     mbar_init(&sh.p_ready, L::kSoft);
     mbar_init(&sh.pv_done, 1);
     mbar_init(&sh.q_ready, L::kSoft);
+    mbar_init(&sh.drained, 1);
     for (int i = 0; i < kJobs; ++i) {
       mbar_init(&sh.job_full[i], 1);
       mbar_init(&sh.seen_full[i], 1);
@@ -569,15 +590,17 @@ __global__ void __launch_bounds__(Layout<R, D>::kThreads, 2)
     // --- jobs, and their tiles into the ring, a page at a time; lane l keeps page l of a window of 32 pages --------------
     const long long end = total * (me + 1) / blocks;
     Walk<R> walk(a, sh.start_b, sh.start_at, end - first);
+    if (lane == 0) sh.share = end - first;
     auto owner = [&](long long u) { return int(((u + 1) * blocks - 1) / total); };
     const int per = kTile / a.page;                       // pages of a tile
-    unsigned it = 0, slot = 0, turn = 0;                  // tiles so far; the next slot and how often the ring went round
-    for (unsigned jobs = 0;; ++jobs) {
+    unsigned filled = 0, slot = 0, turn = 0;              // slots so far; the next one and how often the ring went round
+    bool gone = false;
+    for (unsigned jobs = 0; !gone; ++jobs) {
       const Job g = walk.next(a, end, owner);
       if (g.blocks && lane == 0)
         a.shared[(g.starts ? 0 : kMaxGrid) + me] = SharedItem{g.b, g.h, g.rb * R, g.live, g.first, g.blocks, {0, 0}};
       const unsigned js = jobs % kJobs;
-      if (jobs >= kJobs && !mbar_wait(&sh.job_empty[js], (jobs / kJobs - 1) & 1, dead)) break;
+      if (jobs >= kJobs && __any_sync(~0u, !mbar_wait(&sh.job_empty[js], (jobs / kJobs - 1) & 1, dead))) break;
       if (lane == 0) {
         sh.job[js] = g;
         mbar_arrive(&sh.job_full[js]);
@@ -602,7 +625,7 @@ __global__ void __launch_bounds__(Layout<R, D>::kThreads, 2)
       int pid = page_of(p0), exps = exps_of(pid);
       int next_pid = page_of(p0 + 32), next_exps = kNoPage;
       bool bad = p0 + lane < last && exps == kNoPage;
-      for (int i = 0; i < g.count; ++i, ++it) {
+      for (int i = 0; i < g.count; ++i) {
         const int here = (g.tile + i) * per - p0;                            // the tile's pages are lanes [here, here + per)
         const bool own = lane >= here && lane < here + per;
         const bool load = own && exps != kNoPage;
@@ -610,7 +633,8 @@ __global__ void __launch_bounds__(Layout<R, D>::kThreads, 2)
         const int y = (pid * a.heads + g.h) * a.page;
 #pragma unroll
         for (int side = 0; side < 2; ++side) {
-          if (turn) mbar_wait(&sh.empty[slot], (turn - 1) & 1, dead);
+          gone = __any_sync(~0u, turn && !mbar_wait(&sh.empty[slot], (turn - 1) & 1, dead));
+          if (gone) break;                                  // the slot may still be filled or read
           if (side && own) sh.slot[slot][lane - here] = exps;
           __syncwarp();
           if (lane == 0) mbar_expect(&sh.full[slot], bytes);
@@ -619,7 +643,9 @@ __global__ void __launch_bounds__(Layout<R, D>::kThreads, 2)
             tma_page(side ? &map_v : &map_k, smem(ring + slot * L::kSide) + unsigned((lane - here) * a.page * D),
                      &sh.full[slot], y);
           if (++slot == kSlots) slot = 0, ++turn;
+          ++filled;
         }
+        if (gone) break;
         if (here == 0) next_exps = exps_of(next_pid);
         if (here + per == 32) {
           p0 += 32;
@@ -661,12 +687,10 @@ __global__ void __launch_bounds__(Layout<R, D>::kThreads, 2)
       if (bad && a.status) atomicOr(a.status + g.b, SPEC_ST_BAD_PAGE);
     }
     // the copies in flight land before the block may end
-    for (unsigned k = 0; k < kSlots && k < 2 * it; ++k) {
+    for (unsigned k = 0; k < kSlots && k < filled; ++k) {
       turn -= slot == 0;
       slot = slot == 0 ? kSlots - 1 : slot - 1;
-      const long long t0 = now_ns();
-      while (!mbar_try(&sh.full[slot], turn & 1) && now_ns() - t0 < kWaitNs) {
-      }
+      mbar_drain(&sh.full[slot], turn & 1);
     }
   } else if (warp == kMmaWarp) {
     // --- MMA: one thread issues both products ---------------------------------------------------------------------------
@@ -679,18 +703,18 @@ __global__ void __launch_bounds__(Layout<R, D>::kThreads, 2)
       unsigned n_s = 0, n_p = 0;                           // score products, output products issued
       for (unsigned jobs = 0;; ++jobs) {
         const unsigned js = jobs % kJobs;
-        if (!mbar_wait(&sh.job_full[js], (jobs / kJobs) & 1, dead)) break;
+        if (!mbar_wait(&sh.job_full[js], (jobs / kJobs) & 1, dead) || *dead) break;
         const int count = sh.job[js].count;
         if (count == 0) break;
         mbar_arrive(&sh.job_empty[js]);
-        mbar_wait(&sh.q_ready, jobs & 1, dead);
+        if (!mbar_wait(&sh.q_ready, jobs & 1, dead)) break;
         const unsigned end = n_p + unsigned(count), begin = n_p;
         long long t0 = now_ns();
         for (unsigned poll = 1; n_p < end; ++poll) {
           // scores of the next tile: its keys are there and the last scores have been read
           const unsigned ks = (2 * n_s) % kSlots, kt = (2 * n_s) / kSlots;
-          if (n_s < end && n_s <= n_p + 1 && (mbar_test(&sh.full[ks], kt & 1) || *dead) &&
-              (n_s == 0 || mbar_test(&sh.s_free, (n_s - 1) & 1) || *dead)) {
+          if (n_s < end && n_s <= n_p + 1 && mbar_test(&sh.full[ks], kt & 1) &&
+              (n_s == 0 || mbar_test(&sh.s_free, (n_s - 1) & 1))) {
             tc_after();
             const unsigned k0 = smem(ring + ks * L::kSide);
 #pragma unroll
@@ -705,8 +729,7 @@ __global__ void __launch_bounds__(Layout<R, D>::kThreads, 2)
           }
           // outputs of a tile whose weights are written
           const unsigned vs = (2 * n_p + 1) % kSlots;
-          if (n_p < n_s && (mbar_test(&sh.p_ready, n_p & 1) || *dead) &&
-              (mbar_test(&sh.full[vs], ((2 * n_p + 1) / kSlots) & 1) || *dead)) {
+          if (n_p < n_s && mbar_test(&sh.p_ready, n_p & 1) && mbar_test(&sh.full[vs], ((2 * n_p + 1) / kSlots) & 1)) {
             tc_after();
             const unsigned v0 = smem(ring + vs * L::kSide);
 #pragma unroll
@@ -721,11 +744,14 @@ __global__ void __launch_bounds__(Layout<R, D>::kThreads, 2)
             ++n_p;
             poll = 0;
           }
-          if (poll == 0)
+          if (poll == 0) {
             t0 = now_ns();
-          else if ((poll & 255) == 0 && now_ns() - t0 > kWaitNs)
+          } else if ((poll & 255) == 0 && (*dead || now_ns() - t0 > kWaitNs)) {
             *dead = 1;
+            break;
+          }
         }
+        if (n_p < end) break;
       }
     }
     __syncwarp();
@@ -737,8 +763,7 @@ __global__ void __launch_bounds__(Layout<R, D>::kThreads, 2)
     uint8_t* const p_mine = p_smem + t * 16;
     const int page_shift = 31 - __clz(a.page);
     unsigned n = 0, v_slot = 1, v_turn = 0;                // tiles so far; the slot of the next V and how often the ring went round
-    const bool any = mbar_wait(&sh.job_full[0], 0, dead) && sh.job[0].count > 0;
-    if (tid == 0) sh.more[0] = any;
+    const bool any = __all_sync(~0u, mbar_wait(&sh.job_full[0], 0, dead) && sh.job[0].count > 0);
     if (any) {
       Queries<R, D> q;
       q.load(a, sh.job[0], sh.head[0]);
@@ -746,9 +771,9 @@ __global__ void __launch_bounds__(Layout<R, D>::kThreads, 2)
     }
     fence_async_smem();
     tc_before();
-    softmax_barrier<L::kSoft>();
+    bool go = softmax_all<L::kSoft>(any);                  // (the same in all softmax threads: they meet the same barriers)
     mbar_arrive(&sh.q_ready);
-    for (unsigned jobs = 0; sh.more[jobs & 1]; ++jobs) {   // (one thread's word: all warps meet the same barriers)
+    for (unsigned jobs = 0; go; ++jobs) {
       const unsigned js = jobs % kJobs;
       const Job& g = sh.job[js];
       const int count = g.count;
@@ -893,7 +918,7 @@ __global__ void __launch_bounds__(Layout<R, D>::kThreads, 2)
 
       // --- the next job's queries: their shared memory is free, all score products of this job are done ---------------------
       const unsigned ns = (jobs + 1) % kJobs;
-      const bool more = mbar_wait(&sh.job_full[ns], ((jobs + 1) / kJobs) & 1, dead) && sh.job[ns].count > 0;
+      const bool more = __all_sync(~0u, mbar_wait(&sh.job_full[ns], ((jobs + 1) / kJobs) & 1, dead) && sh.job[ns].count > 0);
       Queries<R, D> q;
       if (more) q.load(a, sh.job[ns], sh.head[(jobs + 1) & 1]);
       // --- the end of this one: the accumulator goes out, normalised or as a partial ---------------------------------------
@@ -941,16 +966,27 @@ __global__ void __launch_bounds__(Layout<R, D>::kThreads, 2)
               part[(r + e) * D] = o;
           }
       }
-      if (tid == 0) sh.more[(jobs + 1) & 1] = more;
       tc_before();
-      softmax_barrier<L::kSoft>();                         // all has been read before the next job writes
-      if (tid == 0) {
-        if (*dead && a.status) atomicOr(a.status + g.b, SPEC_ST_TIMEOUT);
-        mbar_arrive(&sh.job_empty[js]);
-      }
+      go = softmax_all<L::kSoft>(more && !*dead);          // all has been read before the next job writes
+      if (tid == 0) mbar_arrive(&sh.job_empty[js]);
     }
   }
   __syncthreads();
+  if (__builtin_expect(*dead, 0)) {
+    if (tid == 0 && a.status) {
+      int b = sh.start_b;
+      for (long long at = sh.start_at, left = sh.share; left > 0; ++b, at = 0) {
+        const long long units = sequence<R>(a, b).units;
+        if (units > 0) atomicOr(a.status + b, SPEC_ST_TIMEOUT);
+        left -= units - at;
+      }
+    }
+    if (warp == kMmaWarp && lane == 0) {                   // (the thread that issued the products)
+      tc_commit(&sh.drained);
+      mbar_drain(&sh.drained, 0);
+    }
+    __syncwarp();
+  }
   if (warp == kMmaWarp) {
     tc_after();
     asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(tmem), "n"(L::kColumns));
