@@ -562,6 +562,10 @@ __global__ void __launch_bounds__(Layout<R, D>::kThreads, 2)
   };
   for (int b0 = 0; b0 < a.B; b0 += kThreads) total += scan(b0 + tid);
   const int blocks = int(min((long long)(gridDim.x), total));
+  if (a.status && a.num_draft && me == int(gridDim.x) - 1) {    // (counts of sequences without rows, that no job meets, as well)
+    for (int b = tid; b < a.B; b += kThreads)
+      if (a.num_draft[b] < 0 || a.num_draft[b] > a.gmax) atomicOr(a.status + b, SPEC_ST_CLAMPED_GAMMA);
+  }
   if (tid == 0) a.shared[me].blocks = a.shared[kMaxGrid + me].blocks = 0;
   if (me >= blocks) return;
   const long long first = total * me / blocks;
@@ -656,7 +660,7 @@ __global__ void __launch_bounds__(Layout<R, D>::kThreads, 2)
         if (i == 0) {
           // which rows see a token of the block; waited for where a tile holds one
           int nd = a.num_draft ? a.num_draft[g.b] : a.gmax;
-          int bits = nd < 0 || nd > a.gmax ? SPEC_ST_CLAMPED_GAMMA : 0;
+          int bits = 0;
           nd = min(max(nd, 0), a.gmax);
           const unsigned long long all = g.live == 64 ? ~0ull : (1ull << g.live) - 1;
           if (a.parents == nullptr) {
