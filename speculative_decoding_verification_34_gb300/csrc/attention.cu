@@ -1174,7 +1174,9 @@ int dispatch_rows(int R, const AttnArgs& a, const Cache& c, void* ws, cudaStream
 using namespace specverify;
 
 extern "C" size_t spec_attention_workspace_bytes(int B, int gmax, int Hq, int Hkv, int D) {
-  if (B < 0 || gmax < 0 || gmax > SPEC_MAX_TREE_NODES || Hkv < 1 || Hq < Hkv || Hq % Hkv || (D != 64 && D != 128)) return 0;
+  if (B < 0 || gmax < 0 || gmax > SPEC_MAX_TREE_NODES || Hkv < 1 || Hkv > 1024 || Hq < Hkv || Hq % Hkv || Hq / Hkv > 1024 ||
+      (D != 64 && D != 128))
+    return 0;
   const size_t R = size_t(block_rows((gmax + 1) * (Hq / Hkv)));
   return sizeof(SharedItem) * 2 * kMaxGrid + 2 * kMaxGrid * R * (sizeof(float2) + sizeof(float) * size_t(D));
 }
