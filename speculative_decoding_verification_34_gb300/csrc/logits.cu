@@ -192,7 +192,7 @@ __global__ void __launch_bounds__(kThreads, 8) stream_kernel(const LogitsArgs a)
   }
 }
 
-size_t fix_bytes(int window, int entries) { return size_t(window) / 32 * 6 + size_t(entries) * 12; }
+constexpr size_t fix_bytes(int window, int entries) { return size_t(window) / 32 * 6 + size_t(entries) * 12; }
 
 // kStream: the block streams its sequence's rows too; else the launch before has.
 template <class T, int kVec, bool kStream, int kFix>
@@ -438,7 +438,9 @@ LogitsArgs shifted(const LogitsArgs& a, int b0, size_t esz) {
 template <class T, int kVec, bool kStream, int kFix>
 int launch_fix(const LogitsArgs& a, const dim3& grid, cudaStream_t stream) {
   const size_t smem = fix_bytes(a.window, a.entries);
-  const cudaError_t e = cudaFuncSetAttribute(fix_kernel<T, kVec, kStream, kFix>, cudaFuncAttributeMaxDynamicSharedMemorySize, int(smem));
+  // (the most that any call needs: the limit is the kernel's, for all threads that launch it)
+  const cudaError_t e = cudaFuncSetAttribute(fix_kernel<T, kVec, kStream, kFix>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                             int(fix_bytes(kWindow, kEntries)));
   if (e != cudaSuccess) return cuda_fail(e, "logits fix shared memory");
   return launch_early("logits fix kernel launch", fix_kernel<T, kVec, kStream, kFix>, grid, dim3(kFix), smem, stream, a);
 }
