@@ -410,7 +410,8 @@ int spec_apply_stops(int32_t* out_tokens, int32_t* num_accepted, int B, int gmax
  * Ids outside [0,V) in history and draft_tokens count nowhere; lengths are clamped to their
  * arrays.  Limits: gmax <= SPEC_MAX_TREE_NODES, V as for the verify calls, cap <= 2^28.  One
  * launch, or two (the second a programmatic dependent launch) where the logits of a sequence are
- * more than 2048 vectors; no workspace.  Rows go in 16-byte vectors where logits and out lie alike
+ * more than 2048 vectors; no workspace.  The search for marked ids goes by capacities: above cap + gmax + nbias = 12288 it takes a
+ * pass over the history for each 12288 ids of the vocabulary.  Rows go in 16-byte vectors where logits and out lie alike
  * in their 16-byte units (V of any size), else value by value, with the same results.
  */
 int spec_process_logits(const void* logits, void* out, int dtype, int B, int rows, int first_row, int V,

@@ -29,10 +29,12 @@
 // launch joins in a fixed order.
 //
 // Measured (GB300, 32 or 64 query heads, 8 kv heads of 128): 8 sequences of 50-65K tokens, 5 rows: 8 query heads to a kv
-// head (40 rows) 170 us, 5.6 TB/s, bound by the softmax's instructions; 4 or 1 to a kv head (20, 5 rows) 152 us, 6.3 TB/s, 0.93 of
-// the measured copy rate.  64 sequences of 300-4091 tokens, 20 rows: 62 us, 4.8 TB/s (items of 3 to 33 tiles: their starts and
-// ends, and blocks that end apart).  16 trees of 63 nodes at 700-2040 tokens, 256 rows: 83 us, 0.27 PFLOP/s of the
-// operator's products, bound by the softmax of four row blocks.  One sequence of 505 tokens: 9.4 us, all latency.
+// head (40 rows) 170 us, 5.6 TB/s, bound by the softmax's chain for each tile; 4 or 1 to a kv head (20, 5 rows) 148, 151 us, 6.4,
+// 6.3 TB/s, 0.94 of the measured copy rate.  64 sequences of 300-4091 tokens, 20 rows: 61 us, 4.9 TB/s (items of 3 to 33 tiles:
+// their starts and ends, and blocks that end apart).  16 trees of 63 nodes at 700-2040 tokens, 256 rows: 82 us, 0.27 PFLOP/s of
+// the operator's products: the softmax of four row blocks, an instruction issued in half of the cycles and no pipe full (the
+// chain of one tile, barriers and all, with two tiles of an SM's two blocks to hide it).  One sequence of 505 tokens: 9.6 us,
+// all latency.
 // Measured and not kept: one block with two warpgroups on alternate tiles (batch 161 us: their row setup and output stopped
 // both), weights as two e4m3 parts (range 2^-20, reference value raised in 61 % of the tiles), two tiles a step (batch 87 us:
 // the ring holds too little ahead), partials joined by the last block to arrive (batch 69 us, and registers spilled), row

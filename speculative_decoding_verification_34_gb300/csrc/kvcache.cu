@@ -7,8 +7,9 @@
 // the page's earlier tokens have, whose codes are rescaled if it grows.  So what a rejected draft leaves behind is at
 // most a larger exponent of the last page, until that page is written from its start again.
 //
-// Measured (GB300, 8 heads of 128): 8 x 4001 bf16 tokens appended 34 us (4.7 TB/s), 16 x 4095 tokens read back as bf16 64 us
-// (5.2 TB/s), a block of 5 tokens of 128 sequences appended 3.8 us, the paths of 128 trees of 63 nodes kept 4 us.
+// Measured (GB300, 8 heads of 128): 8 x 4001 tokens appended as bf16 32 us (5.0 TB/s), as fp32 44 us (6.1 TB/s), 16 x 4095
+// tokens read back as bf16 63 us (5.3 TB/s), as fp32 100 us; a block of 5 tokens of 128 sequences appended 3.9 us, the
+// paths of 128 trees of 63 nodes kept 6.9 us, of one tree 3.6 us.
 //
 // All three are bound by the bytes they move (at one block of drafts, by the launch).  One group of threads owns one
 // (page, head, K or V) of the pages written, so no two groups share an exponent, and holds the values in registers
@@ -420,8 +421,8 @@ int launch_pages(const AppendArgs& a, int B, cudaStream_t stream) {
 
 // A warp takes a page of at most 16 new tokens, holding up to 8 vectors a lane; a page of more gets as many threads as
 // hold it with 4 vectors each (its 2048 vectors at most: 512 threads), or 8 of bf16 up to 1024 vectors, so that a page
-// is read once whatever its size.  (8 x 4001 tokens of 8 heads of 128 in pages of 64: bf16 37 us with 128 threads of
-// 8 vectors, 40 with 256 of 4; fp32, twice the registers, 57 and 47.)
+// is read once whatever its size.  (8 x 4001 tokens of 8 heads of 128 in pages of 64: bf16 32 us with 128 threads of
+// 8 vectors, 35 with 256 of 4; fp32, twice the registers, 53 and 44.)
 template <class T>
 int launch_append(const AppendArgs& a, int B, cudaStream_t stream) {
   const int vectors = (a.n < a.c.page ? a.n : a.c.page) * a.c.D / kVec;
