@@ -564,12 +564,17 @@ __global__ void __launch_bounds__(Layout<R, D>::kThreads, 2)
   };
   for (int b0 = 0; b0 < a.B; b0 += kThreads) total += scan(b0 + tid);
   const int blocks = int(min((long long)(gridDim.x), total));
-  if (a.status && a.num_draft && me == int(gridDim.x) - 1) {    // (counts of sequences without rows, that no job meets, as well)
-    for (int b = tid; b < a.B; b += kThreads)
-      if (a.num_draft[b] < 0 || a.num_draft[b] > a.gmax) atomicOr(a.status + b, SPEC_ST_CLAMPED_GAMMA);
-  }
   if (tid == 0) a.shared[me].blocks = a.shared[kMaxGrid + me].blocks = 0;
-  if (me >= blocks) return;
+  // Counts out of range, also of sequences without rows, which no job meets: block 0 reports them, once its tiles are on their way.
+  auto report_counts = [&]() {
+    if (me > 0 || !a.status || !a.num_draft) return;
+    for (int b = lane; b < a.B; b += 32)
+      if (a.num_draft[b] < 0 || a.num_draft[b] > a.gmax) atomicOr(a.status + b, SPEC_ST_CLAMPED_GAMMA);
+  };
+  if (me >= blocks) {                                      // (block 0: nobody has rows)
+    if (warp == 0) report_counts();
+    return;
+  }
   const long long first = total * me / blocks;
   long long before = 0;
   for (int b0 = 0; b0 < a.B; b0 += kThreads) {
@@ -692,6 +697,7 @@ __global__ void __launch_bounds__(Layout<R, D>::kThreads, 2)
       }
       if (bad && a.status) atomicOr(a.status + g.b, SPEC_ST_BAD_PAGE);
     }
+    report_counts();
     // the copies in flight land before the block may end
     for (unsigned k = 0; k < kSlots && k < filled; ++k) {
       turn -= slot == 0;
